@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     int g0 = 0;                                // the share's tiles before the job
     uint32_t n = 0;                            // tiles of this half so far
+    bool sat_out = false;                      // it saw nothing of the job before
     Kv8Desc d{0, 0, 0, 0, 0};
     while (!w.done()) {
       if (!w.begins()) d.head_ends = w.ends();
@@ -456,6 +457,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // a thread without a row weighs everything 0
       float ref = row < hf.rows ? 0.0f : 1e30f, sum = 0.0f;
       bool have = row >= hf.rows;              // ref comes from a weight of the row
+      // A parity tells neighbouring rounds of the ring of scales apart, no more, and a half that saw
+      // nothing of the jobs before (few rows, positions before the first token) may be rounds
+      // ahead of the producer.  S of its first tile comes after that tile's scales were written,
+      // and nobody overwrites those before this half's P is there.  (Between two jobs that it
+      // sees, a half sits out three tiles at most, and the parity does.)
+      if (sat_out && hf.lo < hf.hi) wait(&sm.s_full[x][0], n);
+      sat_out = hf.lo >= hf.hi;
       for (int kt = hf.lo; kt < hf.hi; ++kt, ++n) {
         const int g = g0 + kt - (w.tile.kt0 + w.kt);
         const int j0 = kt * kPageRows;
