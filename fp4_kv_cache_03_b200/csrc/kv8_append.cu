@@ -22,6 +22,7 @@ namespace {
 constexpr int kApThreads = 256;
 constexpr int kApCtas = 2;                          // per SM
 constexpr int kApWindow = 64;                       // most tokens of a CTA's window
+constexpr int kApMaxD = 128;                        // most channels of a head, rotated ones too
 
 struct AppendArgs {
   const uint16_t* x[2];                             // k, v
@@ -428,13 +429,15 @@ extern "C" csa2_status_t csa2_kv8_append(const uint16_t* k, int64_t k_stride, co
   auto* kernel = mode == 0   ? kv8_append_kernel<0>
                  : mode == 1 ? kv8_append_kernel<1>
                              : kv8_append_kernel<2>;
-  // angles of the window's reach, of its leaders and of a block's steps
-  const size_t smem = mode ? (size_t)(a.window + kKv8Block - 1 + a.window + kKv8Block) * (a.r.rot / 2) *
-                                 sizeof(float2)
-                           : 0;
+  // Angles of the window's reach, of its leaders and of a block's steps.  The kernel's limit is
+  // every host thread's, so it is always set to the most that any call takes.
+  auto bytes = [](int window, int rot) {
+    return (size_t)(window + kKv8Block - 1 + window + kKv8Block) * (rot / 2) * sizeof(float2);
+  };
+  const size_t smem = mode ? bytes(a.window, a.r.rot) : 0;
   if (smem > 40 * 1024 &&                                 // with the static part, 48 KB need no asking
-      checked(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
+      checked(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)bytes(kApWindow, kApMaxD))) != cudaSuccess)
     return CSA2_ERR_CUDA;
   return launch_pdl(kernel, dim3((unsigned)gx, gy), dim3(kApThreads), smem,
                     (cudaStream_t)stream, a) == cudaSuccess

@@ -212,10 +212,13 @@ extern "C" csa2_status_t csa2_plan_pages(int32_t num_seqs, const int32_t* old_le
   PlanArgs a{num_seqs, old_len, new_len, max_tokens, block_table, max_pages, free_pages, num_free,
              free_used, free_used_out, seq_len, tok_start, q_seq, q_pos, rows,
              static_cast<int*>(workspace)};
-  const size_t smem = ((size_t)num_seqs * 3 + 1) * sizeof(int32_t);
+  // The kernel's limit is every host thread's, so it is always set to the most that any call takes:
+  // a smaller call's own size could come between another thread's setting and its launch.
+  auto bytes = [](int n) { return ((size_t)n * 3 + 1) * sizeof(int32_t); };
+  const size_t smem = bytes(num_seqs);
   if (smem > 40 * 1024 &&                                 // with the static part, 48 KB need no asking
       checked(cudaFuncSetAttribute(plan_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)smem)) != cudaSuccess)
+                                   (int)bytes(kPlanMaxSeqs))) != cudaSuccess)
     return CSA2_ERR_CUDA;
   const int sms = csa2_device_sms();
   // a decode step is all latency, and a small block's barriers are short (64 sequences: 3.6 us with
