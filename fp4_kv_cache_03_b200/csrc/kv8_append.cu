@@ -319,11 +319,9 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) kv8_append_kernel(const _
       float2* const steps = first + nl * half;                               // [16][pair]
       for (int k = warp; k < nl + kKv8Block; k += kApThreads / 32) {
         const double pos = k < nl ? (double)leaders[k].pos : (double)(k - nl);
-        for (int p = lane; p < half; p += 32) {
-          float2 t = rope_turn(a.r, pos, p);
-          if (k >= nl) t = make_float2(t.x / a.r.amplitude, t.y / a.r.amplitude);
-          (k < nl ? first + k * half : steps + (k - nl) * half)[p] = t;
-        }
+        for (int p = lane; p < half; p += 32)
+          (k < nl ? first + k * half : steps + (k - nl) * half)[p] =
+              k < nl ? rope_turn(a.r, pos, p) : rope_unit(a.r, pos, p);
       }
       __syncthreads();
       for (int k = warp; k < nl * kKv8Block; k += kApThreads / 32) {

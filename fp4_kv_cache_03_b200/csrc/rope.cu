@@ -8,6 +8,7 @@
 // 64 x 128 bf16 take 27.7 us (4.84 TB/s), 64 decode rows 4.0 us.
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "rope.cuh"
@@ -250,8 +251,8 @@ extern "C" csa2_status_t csa2_rope_frequencies(const csa2_rope_t* r, double* fre
       r->scaling < CSA2_ROPE_NONE || r->scaling > CSA2_ROPE_PARTS)
     return CSA2_ERR_INVALID_ARG;
   // written so that a NaN fails them
-  if (!(r->theta > 1.0 && r->theta < 1e30) || !(r->amplitude > 0.0 && r->amplitude < 1e6))
-    return CSA2_ERR_INVALID_ARG;
+  if (!(r->theta > 1.0 && r->theta < 1e30)) return CSA2_ERR_INVALID_ARG;
+  if (!(r->amplitude >= FLT_MIN && r->amplitude < 1e6)) return CSA2_ERR_INVALID_ARG;   // fp32 keeps its bits
   if (r->scaling != CSA2_ROPE_NONE && !(r->factor >= 1.0 && r->factor < 1e6))
     return CSA2_ERR_INVALID_ARG;
   if (r->scaling == CSA2_ROPE_BASE && r->rot_dim == 2) return CSA2_ERR_INVALID_ARG;

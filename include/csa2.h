@@ -440,11 +440,11 @@ typedef struct {
   int32_t offset;       /* even, >= 0 */
   int32_t interleaved;  /* 0 or 1 */
   int32_t scaling;      /* csa2_rope_scaling_t */
-  double theta;         /* > 1 */
-  double factor;        /* >= 1; read unless NONE */
-  double orig_len;      /* > 0; PARTS */
-  double slow, fast;    /* slow < fast; PARTS (1 and 32 in the paper) */
-  double amplitude;     /* > 0 */
+  double theta;         /* > 1, < 1e30 */
+  double factor;        /* >= 1, < 1e6; read unless NONE */
+  double orig_len;      /* > 0, < 1e15; PARTS */
+  double slow, fast;    /* 0 <= slow < fast < 1e15; PARTS (1 and 32 in the paper) */
+  double amplitude;     /* >= 2^-126 (fp32's least normal), < 1e6 */
 } csa2_rope_t;
 /* freq[i] = f_i in radians per token, i < rot_dim / 2 (host memory, host arithmetic). */
 CSA2_API csa2_status_t csa2_rope_frequencies(const csa2_rope_t* rope, double* freq);
