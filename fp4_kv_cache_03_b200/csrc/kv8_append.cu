@@ -292,8 +292,16 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) kv8_append_kernel(const _
         ld.count = min(kKv8Block - ld.slot % kKv8Block, end - t);
         const int64_t col = ld.pos / kPageRows;
         ld.page = col < a.max_pages ? __ldg(a.block_table + (int64_t)s * a.max_pages + col) : -1;
-        if (ld.page < 0 || ld.page >= a.num_pages) err = CSA2_ERR_CAPACITY;
+        bool whole = true;                          // the block's tokens all name the sequence
+        if (a.q_seq)
+#pragma unroll
+          for (int i = 1; i < kKv8Block; ++i)
+            if (i < ld.count) whole &= __ldg(a.q_seq + t + i) == s;
+        if (!whole) err = CSA2_ERR_INVALID_ARG;
+        else if (ld.page < 0 || ld.page >= a.num_pages) err = CSA2_ERR_CAPACITY;
         else leaders[atomicAdd(&n_leaders, 1)] = ld;        // any order: blocks are independent
+      } else if (a.q_seq && __ldg(a.q_seq + t - 1) != s) {
+        err = CSA2_ERR_INVALID_ARG;                 // its block's leader does not take it along
       }
     } else if (s != -1) {
       err = CSA2_ERR_INVALID_ARG;

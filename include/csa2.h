@@ -498,7 +498,9 @@ typedef struct {
  *   rope      host, or NULL
  *   A token whose q_seq is outside [-1, num_seqs), that is not among its sequence's rows or
  *   has a negative position is skipped and CSA2_ERR_INVALID_ARG recorded; one without a page
- *   in [0, num_pages) is skipped and CSA2_ERR_CAPACITY recorded.  Two sequences must not
+ *   in [0, num_pages) is skipped and CSA2_ERR_CAPACITY recorded.  A block's new tokens are
+ *   stored together or not at all: where q_seq does not give the same sequence for all of
+ *   them, the block is skipped and CSA2_ERR_INVALID_ARG recorded.  Two sequences must not
  *   share a page that either appends to.
  *   workspace >= csa2_kv8_append_workspace() bytes (status word only) */
 CSA2_API size_t csa2_kv8_append_workspace(void);
