@@ -31,10 +31,13 @@ __device__ __forceinline__ int kv8_least_exp(float amax) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return __half22float2(__half2(h));
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t two) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t two) { return __half22float2(e4m3x2_half2(two)); }
 
 // host checks of a cache argument
 inline csa2_status_t kv8_check(const csa2_kv8_t& c) {

@@ -9,9 +9,11 @@
 // What has to stay precise is split into E4M3 terms instead, on the narrow side:
 //   Q (bf16, 8 significant bits), scaled per row by a power of two so that its largest is in
 //     (224, 448], is hi + lo of 4 bits each: two MMAs into one accumulator;
-//   P = p0 + p1 / 16 + p2 / 256, each remainder scaled by 16 and rounded again: 12 bits, down
-//     to 2^-22 of a row's largest.  The three accumulate in columns of their own (one MMA of 3R
-//     columns) and are added at the end.
+//   P = p0 + p1 / 2^4 + p2 / 2^8 + p3 / 2^15, each remainder scaled by 16, 16 and 128 and rounded
+//     again (none passes 256): a weight is off by at most 2^-11 of itself plus 2^-26 of the row's
+//     largest, and one of 2^-29 of it is not lost yet.  With three terms those under 2^-22 all were,
+//     and tens of thousands of them beside one large weight make up a visible part of the sum.  The
+//     four accumulate in columns of their own (one MMA of 4R columns) and are added at the end.
 // An MMA here costs the read of its A operand (a 128 x 32-byte slice), whatever its N, so the
 // terms are nearly free.  Key scales multiply S; value scales 2^e add e to the exponent's
 // argument, x_j + e_j, and the running reference is the maximum of that sum, so the largest
@@ -34,7 +36,9 @@
 namespace csa2 {
 namespace {
 
-constexpr int kTerms = 3;                      // of P
+constexpr int kTerms = 4;                      // of P
+// what is left of a weight behind term k is scaled by this before it is rounded to term k + 1
+__device__ __forceinline__ constexpr float kv8_step(int k) { return k < 2 ? 16.0f : 128.0f; }
 constexpr float kTopLog2 = 4.0f;               // a fresh reference's weight is 2^4 ...
 constexpr float kGrowLog2 = 4.0f;              // ... and may grow to 2^8 before a rescale
 
@@ -53,7 +57,7 @@ struct DecGeo {
   // with 3 CTAs of 3 units, 214 with 2 of 5.  16 rows need more registers than 3 leave.
   static constexpr int kCtas = kv8_ctas_per_sm(R);
   static constexpr int N = R < 16 ? 16 : R;                 // columns of S^T
-  static constexpr int NP = (kTerms * R + 15) / 16 * 16;    // columns of O^T; those past 3R mean nothing
+  static constexpr int NP = (kTerms * R + 15) / 16 * 16;    // columns of O^T
   static constexpr uint32_t kTmemO = 2 * N;
   static constexpr uint32_t kTmemCols = kv8_cols(2 * N + NP);
   static constexpr uint32_t kP = NP * 128;
@@ -488,14 +492,18 @@ __global__ void __launch_bounds__(DecGeo<R, kUnits>::kThreads, DecGeo<R, kUnits>
             p[k] = ex2(x[c + k] - ((m == -INFINITY ? 0.0f : m) - kTopLog2));
             sum[c + k] = fmaf(p[k], vinv, sum[c + k]);
           }
+          // behind the first term 11 bits of the rest are enough for the other three, and two
+          // columns go in one register
+          uint32_t term = e4m3x2(p[0], p[1]);
+          const float2 v0 = e4m3x2_value(term);
+          __half2 rest = __floats2half2_rn((p[0] - v0.x) * kv8_step(0), (p[1] - v0.y) * kv8_step(0));
 #pragma unroll
           for (int k = 0; k < kTerms; ++k) {
-            const uint32_t term = e4m3x2(p[0], p[1]);
             pb[sw128(k * R + c, key)] = (uint8_t)term;
             pb[sw128(k * R + c + 1, key)] = (uint8_t)(term >> 8);
-            const float2 v = e4m3x2_value(term);
-            p[0] = (p[0] - v.x) * 16.0f;
-            p[1] = (p[1] - v.y) * 16.0f;
+            if (k == kTerms - 1) break;
+            if (k > 0) rest = __hmul2(__hsub2(rest, e4m3x2_half2(term)), __float2half2_rn(kv8_step(k)));
+            term = e4m3x2(rest);
           }
         }
         fence_proxy_async_smem();
@@ -528,7 +536,9 @@ __global__ void __launch_bounds__(DecGeo<R, kUnits>::kThreads, DecGeo<R, kUnits>
         for (int i = 0; i < 8; ++i) {
           const int r = k + i;
           if (r >= rows) continue;
-          const float v = o[0][i] + (o[1][i] + o[2][i] * 0.0625f) * 0.0625f;
+          float v = o[kTerms - 1][i];
+#pragma unroll
+          for (int k = kTerms - 2; k >= 0; --k) v = fmaf(v, 1.0f / kv8_step(k), o[k][i]);
           const float l = (sm.red[0][r] + sm.red[1][r]) + (sm.red[2][r] + sm.red[3][r]);
           if (final) {
             const int64_t hrow = (int64_t)(q_row + r / a.b.G) * a.H + w.h * a.b.G + r % a.b.G;

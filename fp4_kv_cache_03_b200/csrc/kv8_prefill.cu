@@ -10,7 +10,7 @@
 //                           product, with no conversion of K.  A kernel ahead splits all of Q
 //                           into the workspace, and a job's rows come by two TMA boxes (split by
 //                           the softmax warps at each job's start it cost them 8,000 cycles)
-//   O[row, d] += P . V      P in f16 (11 bits, down to 2^-25 of the reference's weight of 1),
+//   O[row, d] += P . V      P in f16 (11 bits, down to 2^-28 of the reference's weight),
 //                           written over S in tensor memory; V's codes widened to f16 (exact)
 //                           by four warps, once per tile for both halves
 // P has 128 x 128 values per tile, V 128 x D for twice as many products: splitting P into E4M3
@@ -18,8 +18,8 @@
 // S and P go in two parts of 64 keys: while one part is weighed, the MMAs of the other part and of
 // the other half run.  S of a part's next tile is issued right behind its P . V, which reads P from
 // the columns that S overwrites; MMAs of one thread run in order.  Scales as in the decode kernel: 2^ek multiplies S, ev is added to the
-// exponent, the sum takes w * 2^-ev.  A row's reference moves only when a weight would pass
-// 2^15: O is rescaled then, by the row's own warp.
+// exponent, the sum takes w * 2^-ev.  A row's reference moves only when weights come near f16's
+// largest: O is rescaled then, by the row's own warp.
 //
 // 2,048 queries over 10,240 tokens, 64 heads on 8 of 128: 718 us, 862 TFLOP/s; the tensor pipe and
 // the exponential unit are both 40% busy, the rest is the softmax warps' latencies (2 such warps
@@ -33,7 +33,9 @@ namespace {
 
 constexpr int kPfThreads = 512;               // 8 softmax warps, 4 converters, producer, issuer, 2 idle
 constexpr int kKStages = 3, kVStages = 2, kHBufs = 2;
-constexpr float kPfMost = 15.0f;              // a fresh reference's weight is 2^0; none grows past 2^15
+constexpr float kPfTop = 3.0f;                // a fresh reference's weight is 2^3 ...
+constexpr float kPfSum = 65000.0f;            // ... and 16 neighbouring ones sum to no more than this
+constexpr float kPfRaise = 10.0f;             // log2 of a weight that is taken to 2^3 when they do
 
 constexpr uint32_t kOffQ = 0;                 // [hi, lo][256 rows][128 B]
 constexpr uint32_t kOffK = kOffQ + 4 * kUnit;
@@ -518,12 +520,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (__any_sync(0xffffffffu, !have)) {  // nothing of O, sum or P depends on ref yet
             const float m = largest();
             if (!have && m > -INFINITY) {
-              ref = m;
+              ref = m - kPfTop;
               have = true;
             }
           }
           // Weights under the reference as f16, their sum, and whether one may be over the limit:
-          // 16 of them sum to more than 2^15 only where one is over 2^11, so no maximum is needed.
+          // 16 of them sum to more than 65,000 only where one is over 2^11.9, so no maximum is needed,
+          // and where they do not, none is past f16's 65,504.  A fresh reference's weight of 2^3
+          // keeps the small weights of long contexts (2^0 would lose those of 2^-25 of the largest);
+          // more would move references too often (2,048-token chunk: 2^0 711 us, 2^3 718, 2^4 722).
           // A part's body is as much as pays to unroll: over the whole tile it outgrows the
           // instruction caches (18% slower), over half a part its latencies show.
           uint32_t p[32];
@@ -551,13 +556,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               add = fmaf(v.x + v.y, inf.vinv[part * 4 + b], add);
               most = fmaxf(most, v.x + v.y);
             }
-            return most > 32768.0f;                  // 2^kPfMost
+            return most > kPfSum;
           };
 #pragma unroll 1
           while (__any_sync(0xffffffffu, weigh())) {
             // rarely: raise the reference, take sum and O along, and weigh the part again
             const float m = largest();
-            const float up = m - ref > kPfMost - 5.0f ? ceilf(m - ref) : 0.0f;
+            const float up = m - ref > kPfRaise ? ceilf(m - ref) - kPfTop : 0.0f;
             const float alpha = ex2(-up);
             ref += up;
             sum *= alpha;

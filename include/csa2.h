@@ -515,11 +515,13 @@ CSA2_API csa2_status_t csa2_kv8_append(const uint16_t* k, int64_t k_stride, cons
  * query i is at position t = seq_len[s] - n_s + i and sees positions max(0, t - window + 1)
  * .. t (window 0: 0 .. t; t < 0: none).  Query head h reads KV head h / (H / H_kv).
  *   l_j = softmax_scale * q . k_j;  out = sum_j softmax(l)_j v_j;  lse = log(sum_j exp(l_j))
- * (natural log); no positions at all gives out = 0, lse = -inf.  Accumulation, maximum and
- * sum are fp32; out is rounded to bf16 once.  Each row of q is scaled by a power of two and
- * split into two E4M3 terms: elements of at least 2^-9 of the row's largest are exact, a
- * smaller one is off by at most 2^-17 of the largest.  Rows of out and lse at and after
- * q_start[num_seqs] are not written.
+ * (natural log); no positions at all gives out = 0, lse = -inf.  Logits, maximum, sums and the
+ * accumulation of out are fp32, and out is rounded to bf16 once.  Before that two operands are
+ * rounded: the weights w_j = exp(l_j) 2^ev_j that meet V's codes, by at most 2^-11 of themselves
+ * plus 2^-26 of the row's largest (the sum of the softmax takes them unrounded), and Q, whose
+ * rows are scaled by a power of two and split into two E4M3 terms: elements of at least 2^-9 of
+ * the row's largest are exact, a smaller one is off by at most 2^-17 of the largest.  Rows of out
+ * and lse at and after q_start[num_seqs] are not written.
  *   q         device bf16 [num_q][H][D], rows q_stride elements apart (a multiple of 8,
  *             >= H * D), 16-byte aligned
  *   seqs      seq_len, block_table and, with a NULL q_start, q_per_seq are read (q_seq is

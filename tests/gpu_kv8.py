@@ -17,7 +17,8 @@ def check(st, lens, new, table, q, window, scale, out, lse, least=2.0 ** -22):
       lse    d + 2^-20 |lse|
       out    2^-8 |out| + (2^-11 + 2 d) * sum p |v| + least * max_j(p_j 2^e_j) * sum |code|:
     fp32 sums, Q's second term, the fp32 exponent, one rounding to bf16, and weights w 2^e that are
-    off by at most 2^-12 of themselves or ``least`` of the row's largest."""
+    off by at most 2^-11 of themselves (2^-14 from 2^-10 of the largest on in the decode kernel) and
+    ``least`` of the row's largest."""
     t = 0
     D, G = st.D, q.shape[1] // st.H
     for s, (n_len, n) in enumerate(zip(lens, new)):
