@@ -397,14 +397,20 @@ CSA2_API csa2_status_t csa2_scatter_rows(const uint8_t* src, int32_t row_bytes, 
  *   q_pos     device int64 [max_tokens]    its position in the sequence
  *   rows      device int64 [max_tokens]    its cache row, as csa2_quant_append's dst_row
  *   free_used_out device int32 [1]         entries of free_pages taken so far
- * Tokens behind the last sequence's get -1 in the three maps.  A sequence is granted nothing
- * -- its seq_len stays old_len, its tokens get -1 in the maps, and CSA2_ERR_CAPACITY is
- * recorded -- when its pages exceed block_table's max_pages columns, its tokens exceed
- * max_tokens, or it needs pages and those of the sequences up to and including it exceed the
- * list (a sequence refused for the first two reasons takes no pages, one refused for the
- * third counts).  Negative lengths, and a free_used outside [0, num_free], are taken as 0
- * (as an empty list, for free_used) and CSA2_ERR_INVALID_ARG is recorded.  A page < 0 in a
- * table or the list gives row -1 and CSA2_ERR_CAPACITY.
+ * Tokens behind the last sequence's get -1 in the three maps.  csa2_kv8_append and
+ * csa2_kv8_attn pass over them; csa2_quant_append, the indexer and csa2_sparse_attn report
+ * every one as an error, so give those calls the step's tokens alone: tok_start[num_seqs] of
+ * them. (The maps count entries.  Where a cache keeps one per several tokens, as behind
+ * csa2_compress_append, csa2_sparse_attn's q_pos is the token's position, not this one.) A
+ * sequence is granted nothing -- its seq_len stays old_len, its tokens get -1 in the maps,
+ * and CSA2_ERR_CAPACITY is recorded -- when its pages exceed block_table's max_pages
+ * columns, its tokens exceed max_tokens, or it needs pages and those of the sequences up to
+ * and including it exceed the list (a sequence refused for the first two reasons takes no
+ * pages, one refused for the third counts).  csa2_kv8_attn, which goes by tok_start and
+ * seq_len, still answers a refused sequence's queries, as if they were those of its latest
+ * stored entries: drop these rows. Negative lengths, and a free_used outside [0, num_free],
+ * are taken as 0 (as an empty list, for free_used) and CSA2_ERR_INVALID_ARG is recorded.  A
+ * page < 0 in a table or the list gives row -1 and CSA2_ERR_CAPACITY.
  *   1 <= num_seqs <= 16384; 1 <= max_tokens <= 2^30; 1 <= max_pages < 2^24; q_seq, q_pos and
  *   rows 16-byte aligned.  No output may overlap an input or another output, but block_table
  *   is updated in place.  workspace >= csa2_plan_pages_workspace() bytes. */
