@@ -5,11 +5,12 @@
 // their largest magnitude, the block's exponent, rescales the older codes if that grew, and
 // writes the new ones.  A block belongs to the CTA whose window of consecutive tokens holds
 // its first new token (its leader).  The window grows from 1 to 64 tokens with the batch: a
-// decode token leads its own block and spreads over the GPU, a prefill fills it with one wave
-// of CTAs that each look up their tokens, compute their angles once for all heads, and then
-// stream.  No two warps ever touch the same block.  Bound by HBM for prefills (2 bytes read and
-// 1 written per value), by latency for decodes: 17,300 rotated tokens of 8 heads of 128 take 36 us
-// (2.95 TB/s; issue is half used, 16 warps per SM), 64 decodes 6.3 us.
+// decode token leads its own block and spreads over the GPU, a prefill fills it with two waves
+// of CTAs (and up to a few CTAs more, as windows are rounded down) that each look up their tokens,
+// compute their angles once for all heads, and then stream.  No two warps ever touch the same
+// block.  A prefill has to move 2 bytes in and 1 out per value; what bounds it is the warps' own
+// latency: 122 registers leave 16 warps per SM, which use half of the issue slots.  17,300 rotated
+// tokens of 8 heads of 128 take 36.5 us (2.91 TB/s).  Decodes are a chain of look-ups: 64 take 6.3 us.
 //
 // A lane's item is two vectors of 8 channels of one token, chosen so that the pairs of either
 // rotary layout lie inside it: neighbours, or channels i .. and i + rot / 2 .. .
@@ -420,7 +421,8 @@ extern "C" csa2_status_t csa2_kv8_append(const uint16_t* k, int64_t k_stride, co
   a.status = static_cast<int*>(workspace);
   // Two waves of CTAs before windows and head groups grow: with one wave the CTA with the most
   // blocks decides (17,300 tokens of 8 heads: 43 us; two waves 36, four waves of 16-token windows,
-  // whose look-ups and angles serve fewer tokens, 65).
+  // whose look-ups and angles serve fewer tokens, 65).  Windows and head groups are rounded down, so
+  // the grid is at least that: 597 CTAs for those tokens on 592 places.
   const int64_t want = 2 * kApCtas * (int64_t)(csa2_device_sms() > 0 ? csa2_device_sms() : 148);
   const int64_t units = (int64_t)num_tokens * cache.H_kv;
   a.window = (int)(units / want < 1 ? 1 : units / want > kApWindow ? kApWindow : units / want);

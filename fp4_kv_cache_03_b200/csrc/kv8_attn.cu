@@ -27,8 +27,8 @@
 // split the next job's Q.  K and V tiles alternate in a ring of 16 KB units in the order that
 // the MMAs consume them: K0 K1 V0 K2 V1 ..., so S of tile t+1 runs under the softmax of tile t.
 //
-// One token over 1,048,576 tokens, 64 heads on 8 of 128: 341 us (6.3 TB/s); 64 ragged decodes over
-// 485,000 tokens: 206 us.
+// One token over 1,048,576 tokens, 64 heads on 8 of 128: 341 to 346 us (6.2 to 6.3 TB/s); 64 ragged
+// decodes over 485,000 tokens: 208 us.
 #include <cudaTypedefs.h>
 
 #include "kv8_attn.cuh"
@@ -708,8 +708,10 @@ bool kv8_q_map(CUtensorMap* m, const Kv8AttnArgs& a) {
 namespace {
 
 // Rows of a job: the least template that holds the batch's mean queries per sequence times the
-// heads of a KV head; above 16 the prefill kernel.  64 sequences of 8,192 keys, 4 KV heads: 8 rows
-// 105 us here, 16 rows 140 (prefill kernel: 237), 32 rows 360 (prefill kernel: 247).
+// heads of a KV head; above 16 the prefill kernel.  The mean is of what the host knows, the rows of
+// q and the sequences, spare and idle ones included.  64 sequences of 8,192 keys, 4 KV heads: 8 rows
+// 100 us here, 16 rows 138 (prefill kernel: 222), 32 rows 360 when there was a template for them
+// (prefill kernel: 224).
 int kv8_rows(int num_q, int num_seqs, int G) {
   const int64_t rows = ((int64_t)num_q + num_seqs - 1) / num_seqs * G;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : kPrefillRows;

@@ -1,7 +1,7 @@
 // Causal attention over the paged 8-bit cache, for many query rows per KV head (prefill).
 //
-// Bound by the tensor cores and, as closely, by the exponentials: a 128 x 128 tile of S costs
-// 1,024 cycles of MMAs (below) and 1,024 of the SM's 16 ex2 per cycle.
+// What it cannot do without are the tensor cores and, as much, the exponentials: a 128 x 128 tile of
+// S costs 1,024 cycles of MMAs (below) and 1,024 of the SM's 16 ex2 per cycle.
 //
 // A job is 256 rows (queries x the G heads of one KV head) in two halves of 128, each with a
 // softmax warpgroup of one thread per row, so that neither maximum nor sum crosses threads.
@@ -17,13 +17,13 @@
 // terms as the decode kernel does would cost three conversions per value here.
 // S and P go in two parts of 64 keys: while one part is weighed, the MMAs of the other part and of
 // the other half run.  S of a part's next tile is issued right behind its P . V, which reads P from
-// the columns that S overwrites; MMAs of one thread run in order.  Scales as in the decode kernel: 2^ek multiplies S, ev is added to the
-// exponent, the sum takes w * 2^-ev.  A row's reference moves only when weights come near f16's
-// largest: O is rescaled then, by the row's own warp.
+// the columns that S overwrites; MMAs of one thread run in order.  Scales as in the decode kernel:
+// 2^ek multiplies S, ev is added to the exponent, the sum takes w * 2^-ev.  A row's reference moves
+// only when weights come near f16's largest: O is rescaled then, by the row's own warp.
 //
-// 2,048 queries over 10,240 tokens, 64 heads on 8 of 128: 718 us, 862 TFLOP/s; the tensor pipe and
-// the exponential unit are both 40% busy, the rest is the softmax warps' latencies (2 such warps
-// per scheduler).
+// 2,048 queries over 10,240 tokens, 64 heads on 8 of 128: 718 to 727 us, 861 to 850 TFLOP/s; the
+// tensor pipe and the exponential unit are both 40% busy, and what bounds it are the softmax warps'
+// latencies (2 such warps per scheduler).
 #include <cuda.h>
 
 #include "kv8_attn.cuh"

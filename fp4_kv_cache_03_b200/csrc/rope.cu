@@ -224,7 +224,8 @@ cudaError_t rope_launch(RopeCall& a, cudaStream_t st) {
   const int half = a.r.rot / 2;
   const int per_head = mode == 0 ? a.D - half : mode == 1 ? a.D / V : (a.D - half) / V;
   const int64_t per_row = (int64_t)per_head * a.heads;
-  // eight CTAs per SM before they grow to kRopeItems
+  // CTAs for eight per SM before they grow to kRopeItems (registers let 4 to 8 run at a time, 4 of
+  // the bf16 form in two halves)
   const int sms = csa2_device_sms() > 0 ? csa2_device_sms() : 148;
   const int64_t even = per_row * a.rows / (8 * sms);
   const int items = even < kRopeThreads ? kRopeThreads : even > kRopeItems ? kRopeItems : (int)even;

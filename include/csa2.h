@@ -541,7 +541,14 @@ CSA2_API csa2_status_t csa2_kv8_append(const uint16_t* k, int64_t k_stride, cons
  *   CSA2_ERR_CAPACITY recorded.
  *   workspace >= csa2_kv8_attn_workspace(...) bytes of the same sizes (a call with fewer queries
  *             per sequence or more sequences may need another size, not always a smaller one;
- *             for prefills it holds a copy of q in 256 bytes per row) */
+ *             for prefills it holds a copy of q in 256 bytes per row)
+ *   Two kernels serve the call, and num_q / num_seqs, rounded up, times H / H_kv picks one for
+ *   the whole batch: up to 16 one for decoding, which takes few queries of a sequence at a time
+ *   and reads its keys for each such group, above 16 one for prefilling, in jobs of 256 rows.
+ *   q_start is not seen by this choice: spare rows of q and idle sequences count.  Any batch is
+ *   right; a long chunk among many decoding or idle sequences, or single tokens in a q of many
+ *   spare rows, is slow in the kernel that it gets: give such a batch in two calls, one over the
+ *   chunks' sequences and one over the decoding ones. */
 CSA2_API size_t csa2_kv8_attn_workspace(int32_t num_q, int32_t num_seqs, int32_t H, int32_t H_kv,
                                         int32_t D);
 CSA2_API csa2_status_t csa2_kv8_attn(const uint16_t* q, int64_t q_stride, int32_t num_q, int32_t H,
