@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) kv8_append_kernel(const _
       const int begin = a.q_seq ? __ldg(a.tok_start + s) : s * a.q_per_seq;
       const int end = a.q_seq ? __ldg(a.tok_start + s + 1) : begin + a.q_per_seq;
       ld.pos = (int64_t)__ldg(a.seq_len + s) - end + t;
-      if (t < begin || t >= end || end > a.num_tokens || ld.pos < 0) {
+      if (begin < 0 || t < begin || t >= end || end > a.num_tokens || ld.pos < 0) {
         err = CSA2_ERR_INVALID_ARG;
       } else if (ld.pos % kKv8Block == 0 || t == begin) {
         ld.slot = (int)(ld.pos % kPageRows);

@@ -49,3 +49,16 @@ def test_only_that_block_is_left_out(csa2, T, H, at):  # noqa: F811
                 R.append(kept_c, kept_e, v[a:b], [0, b - a], [first + b], table)
         np.testing.assert_array_equal(got_c[kv], kept_c)
         np.testing.assert_array_equal(got_e[kv], kept_e)
+
+
+@pytest.mark.parametrize("start", [[-5, 6, 6], [-1, 6, 6], [-(2 ** 31), 6, 6]])
+@pytest.mark.parametrize("length", [6, 11, 16])
+def test_rows_that_start_before_the_first_are_refused(csa2, start, length):  # noqa: F811
+    st = Store(csa2, 3, 1, 16, fill=0)
+    x = torch.ones(6, 1, 16, device="cuda", dtype=torch.bfloat16)
+    before = st.host()
+    seqs = csa2.make_seqs(None, _i32([length, 2]), q_seq=_i32([0] * 6), block_table=_i32([[2, -1], [1, -1]]))
+    csa2.kv8_append(x, x, st.cache, seqs, _i32(start), st.ws)
+    assert csa2.status_fetch(st.ws) == csa2.ERR_INVALID_ARG
+    after = st.host()
+    assert all(np.array_equal(a, b) for u, v in zip(before, after) for a, b in zip(u, v))
