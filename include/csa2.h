@@ -436,8 +436,9 @@ CSA2_API csa2_status_t csa2_plan_pages(int32_t num_seqs, const int32_t* old_len,
  *           g = clamp((turns_i - slow) / (fast - slow), 0, 1):  g f_i + (1 - g) f_i / factor
  * (PARTS is the "NTK-by-parts" interpolation of Peng et al., "YaRN: Efficient Context Window
  * Extension of Large Language Models", 2023.)  The angle is reduced to a fraction of a turn
- * in fp64, so positions in the millions keep fp32 accuracy; the products are fp32, rounded
- * once. */
+ * in fp64 and rounded to fp32 there, so positions in the millions keep fp32 accuracy; sine,
+ * cosine and products are fp32: y is off by at most 2^-21 of (|x_a| + |x_b|) * amplitude, and
+ * rounded to its type once. */
 typedef enum {
   CSA2_ROPE_NONE = 0, CSA2_ROPE_LINEAR = 1, CSA2_ROPE_BASE = 2, CSA2_ROPE_PARTS = 3
 } csa2_rope_scaling_t;
@@ -487,7 +488,8 @@ typedef struct {
 /* Quantise + append the step's tokens.  Sequence s's n_s = tok_start[s + 1] - tok_start[s]
  * tokens are rows tok_start[s] .. of k and v and take positions seq_len[s] - n_s ..
  * seq_len[s] - 1 (seqs.seq_len counts them already, as csa2_plan_pages writes it).  With a
- * rope the keys are rotated at those positions first, in fp32 (offset + rot_dim <= D).  Per
+ * rope the keys are rotated at those positions first, in fp32 (offset + rot_dim <= D; to 2^-20
+ * of (|x_a| + |x_b|) * amplitude, as angles within a block come from its first one's).  Per
  * 16-token block and head, K and V apart:
  *   e    = the least integer with amax <= 448 * 2^e over the block's new tokens, at least the
  *          block's e while it holds older tokens, within [-60, 60]
