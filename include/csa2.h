@@ -437,7 +437,8 @@ CSA2_API csa2_status_t csa2_plan_pages(int32_t num_seqs, const int32_t* old_len,
  * (PARTS is the "NTK-by-parts" interpolation of Peng et al., "YaRN: Efficient Context Window
  * Extension of Large Language Models", 2023.)  The angle is reduced to a fraction of a turn
  * in fp64 and rounded to fp32 there, so positions in the millions keep fp32 accuracy; sine,
- * cosine and products are fp32: y is off by at most 2^-21 of (|x_a| + |x_b|) * amplitude, and
+ * cosine and products are fp32: up to positions of 2^31, y is off by at most 2^-21 of
+ * (|x_a| + |x_b|) * amplitude (further out the angle's own 2^-52 of itself shows), and it is
  * rounded to its type once. */
 typedef enum {
   CSA2_ROPE_NONE = 0, CSA2_ROPE_LINEAR = 1, CSA2_ROPE_BASE = 2, CSA2_ROPE_PARTS = 3
